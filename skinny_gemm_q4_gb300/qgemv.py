@@ -551,14 +551,16 @@ def _need(ok: bool, what: str):
 
 def _heads(t, name: str, heads: int, dim: int, N: int):
     """(pointer, token stride) of an fp16 CUDA tensor [N][heads][dim] (or
-    [N][heads * dim]) whose tokens may be strided."""
+    [N][heads * dim]) whose tokens may be strided.  (Tokens that all lie in one
+    place, as expand() makes them, are refused: a stride of 0 means contiguous
+    to the library.)"""
     if t.shape == (N, heads, dim):
         s, h, d = t.stride()
         ok = N == 0 or (d == 1 and (h == dim or heads == 1))
     else:
         ok = t.shape == (N, heads * dim) and (N == 0 or t.stride(1) == 1)
         s = t.stride(0) if ok else 0
-    if not (ok and t.is_cuda and t.dtype is sys.modules["torch"].float16):
+    if not (ok and (s or N < 2) and t.is_cuda and t.dtype is sys.modules["torch"].float16):
         raise ValueError(f"{name}: a CUDA fp16 tensor [{N}][{heads}][{dim}] expected, tokens "
                          "contiguous")
     return t.data_ptr(), (s if N > 1 else 0)

@@ -1,0 +1,69 @@
+"""What the binding refuses before a call reaches the library (no GPU needed:
+CPU tensors that say they are on one, and handles that are never used)."""
+import pytest
+import torch
+
+
+class Fake:
+    """A CPU tensor that a call takes for one on the GPU."""
+
+    def __init__(self, t):
+        self.t = t
+
+    is_cuda = True
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def half(*shape):
+    return Fake(torch.zeros(shape, dtype=torch.float16))
+
+
+def ints(*shape, dtype=torch.int32):
+    return Fake(torch.zeros(shape, dtype=dtype))
+
+
+@pytest.fixture(scope="module")
+def qg():
+    from skinny_gemm_q4_gb300 import build, qgemv
+    build.build()
+    qgemv.load()
+    return qgemv
+
+
+@pytest.fixture
+def cache(qg):
+    c = object.__new__(qg.KVCache)
+    c.c, c.kv_heads, c.head_dim = None, 2, 64
+    return c
+
+
+def attn_call(qg, cache, N=1, H=4, D=64, **change):
+    args = dict(q=half(N, H, D), out=half(N, H, D), q_start=ints(2), kv_len=ints(1),
+                page_table=ints(1, 3), max_q=N)
+    return qg.make_attn_call(cache, **{**args, **change})
+
+
+def test_broadcast_tokens_are_refused(qg, cache):
+    """Tokens that share their storage (stride 0) are not taken for contiguous
+    ones, which lie beyond it."""
+    wide = Fake(torch.zeros((1, 4, 64), dtype=torch.float16).expand(3, 4, 64))
+    flat = Fake(torch.zeros((1, 256), dtype=torch.float16).expand(3, 256))
+    kv = Fake(torch.zeros((1, 2, 64), dtype=torch.float16).expand(3, 2, 64))
+    for bad in (dict(q=wide), dict(out=wide), dict(out=flat)):
+        with pytest.raises(ValueError):
+            attn_call(qg, cache, N=3, **bad)
+    for q, k, more in ((wide, half(3, 2, 64), {}), (half(3, 4, 64), kv, {}),
+                       (half(3, 4, 64), half(3, 2, 64), dict(q_out=wide)),
+                       (half(3, 4, 64), half(3, 2, 64),
+                        dict(cache=cache, slots=ints(3, dtype=torch.int64), v=kv))):
+        with pytest.raises(ValueError):
+            qg.make_rope_call(q, k, ints(3), **more)
+    slots = ints(3, dtype=torch.int64)
+    with pytest.raises(ValueError):
+        cache.write(kv, half(3, 2, 64), slots)
+    with pytest.raises(ValueError):
+        cache.read(slots, half(3, 2, 64), kv)
+    attn_call(qg, cache, N=1, q=Fake(torch.zeros((1, 4, 64), dtype=torch.float16).expand(1, 4, 64)))
+    assert attn_call(qg, cache, N=3).args.q_stride == 256
