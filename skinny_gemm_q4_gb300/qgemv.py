@@ -32,6 +32,7 @@ FLAG_NO_FALLBACK = 4
 FLAG_MMA_SYNC_PREFILL = 8
 
 OK = 0
+EINVAL = -1
 STATUS_NAMES = {0: "QG_OK", -1: "QG_EINVAL", -2: "QG_EUNSUPPORTED", -3: "QG_EALIGN",
                 -4: "QG_ECUDA", -5: "QG_ENOMEM", -6: "QG_EFAULT_INJECTED"}
 
@@ -574,10 +575,17 @@ def _ints(t, name: str, n, dtype):
 
 class _Call:
     """A prepared call: the C arguments and the tensors that they point to.
-    It can be run any number of times (the tensors' contents may change)."""
+    It can be run any number of times (the tensors' contents may change), on
+    handles of its q heads' number and size, `heads`: the library goes by the
+    handle's and cannot see the tensors'."""
 
-    def __init__(self, args, *keep):
-        self.args, self.ref, self.keep = args, ctypes.byref(args), keep
+    def __init__(self, args, heads, *keep):
+        self.args, self.ref, self.heads, self.keep = args, ctypes.byref(args), heads, keep
+
+
+def _other_heads(what: str, call: _Call, handle: str):
+    raise QgemvError(EINVAL, what, f"the call has heads {call.heads[0]} x {call.heads[1]}, "
+                                   f"the handle is for {handle}")
 
 
 class KVCache:
@@ -675,10 +683,11 @@ def make_rope_call(q, k, positions, q_out=None, k_out=None, q_weight=None, k_wei
             setattr(a, name, w.data_ptr())
     a.positions = _ints(positions, "positions", N, torch.int32)
     if cache is not None:
+        _need(slots is not None and v is not None, "a cache needs slots and v")
         a.cache = cache.c
         a.slots = _ints(slots, "slots", N, torch.int64)
         a.v, a.v_stride = _heads(v, "v", cache.kv_heads, D, N)
-    return _Call(a, q, k, q_out, k_out, q_weight, k_weight, positions, cache, slots, v)
+    return _Call(a, (H, D), q, k, q_out, k_out, q_weight, k_weight, positions, cache, slots, v)
 
 
 class Rope:
@@ -700,6 +709,8 @@ class Rope:
             pass
 
     def run(self, call: _Call, stream=None):
+        if call.heads[1] != self.desc.head_dim:
+            _other_heads("qgemv_rope_run", call, f"heads of {self.desc.head_dim}")
         st = _lib.qgemv_rope_run(self.r, call.ref, _stream_ptr(stream))
         if st:
             _check(st, "qgemv_rope_run")
@@ -712,6 +723,7 @@ def make_attn_call(cache: KVCache, q, out, q_start, kv_len, page_table, max_q: i
     whose pages are page_table[b]; out as q, lse fp32 [N][q_heads] or None."""
     import torch
     N, H, D = q.shape
+    _need(D == cache.head_dim, f"q: heads of {D}, the cache's are of {cache.head_dim}")
     B = kv_len.shape[0]
     a = QgAttnArgs()
     a.cache, a.N, a.B, a.max_q = cache.c, N, B, max_q
@@ -732,7 +744,7 @@ def make_attn_call(cache: KVCache, q, out, q_start, kv_len, page_table, max_q: i
     a.table_stride = page_table.stride(0) if B > 1 else 0
     a.scale = D ** -0.5 if scale is None else scale
     a.causal, a.window = int(causal), window
-    return _Call(a, cache, q, out, q_start, kv_len, page_table, lse)
+    return _Call(a, (H, D), cache, q, out, q_start, kv_len, page_table, lse)
 
 
 class Attn:
@@ -741,6 +753,7 @@ class Attn:
 
     def __init__(self, q_heads: int, kv_heads: int, head_dim: int, max_tokens: int,
                  max_len: int, max_batch: int = None):
+        self.heads = q_heads, head_dim
         self.a = qgemv_attn_create(QgAttnDesc(q_heads, kv_heads, head_dim, max_tokens,
                                               min(max_tokens, 65535) if max_batch is None
                                               else max_batch, max_len))
@@ -757,6 +770,8 @@ class Attn:
             pass
 
     def run(self, call: _Call, stream=None):
+        if call.heads != self.heads:
+            _other_heads("qgemv_attn_run", call, "%d x %d" % self.heads)
         st = _lib.qgemv_attn_run(self.a, call.ref, _stream_ptr(stream))
         if st:
             _check(st, "qgemv_attn_run")

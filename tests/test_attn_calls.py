@@ -1,5 +1,7 @@
 """What the binding refuses before a call reaches the library (no GPU needed:
 CPU tensors that say they are on one, and handles that are never used)."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -67,3 +69,28 @@ def test_broadcast_tokens_are_refused(qg, cache):
         cache.read(slots, half(3, 2, 64), kv)
     attn_call(qg, cache, N=1, q=Fake(torch.zeros((1, 4, 64), dtype=torch.float16).expand(1, 4, 64)))
     assert attn_call(qg, cache, N=3).args.q_stride == 256
+
+
+def test_calls_of_other_heads_than_the_handle_are_refused(qg, cache):
+    """A call carries no head sizes of its own to the library, which goes by the
+    handle's: single tokens of fewer or smaller heads would be read past
+    their end."""
+    def refused(handle, call):
+        with pytest.raises(qg.QgemvError) as e:
+            handle.run(call, stream=SimpleNamespace(cuda_stream=0))
+        return e.value.status == -1 and "heads" in str(e.value)
+
+    a = object.__new__(qg.Attn)
+    a.a = None
+    for a.heads in ((32, 64), (4, 128), (2, 64)):
+        for N in (1, 2):
+            assert refused(a, attn_call(qg, cache, N, 4, 64))
+    r = object.__new__(qg.Rope)
+    r.r, r.desc = None, qg.rope_desc(128)
+    for N in (1, 2):
+        assert refused(r, qg.make_rope_call(half(N, 4, 64), half(N, 2, 64), ints(N)))
+    with pytest.raises(ValueError):  # other heads than the cache's
+        attn_call(qg, cache, D=128)
+    for slots in (None, ints(1, dtype=torch.int64)):
+        with pytest.raises(ValueError):  # a cache, and no slots or no values
+            qg.make_rope_call(half(1, 4, 64), half(1, 2, 64), ints(1), cache=cache, slots=slots)
