@@ -579,11 +579,16 @@ class _Call:
     handles of its q heads' number and size, `heads`: the library goes by the
     handle's and cannot see the tensors'."""
 
-    def __init__(self, args, heads, *keep):
-        self.args, self.ref, self.heads, self.keep = args, ctypes.byref(args), heads, keep
+    def __init__(self, args, heads, cache, *keep):
+        self.args, self.ref, self.heads, self.cache = args, ctypes.byref(args), heads, cache
+        self.keep = keep
 
 
-def _other_heads(what: str, call: _Call, handle: str):
+def _unfit(what: str, call: _Call, handle: str):
+    """Refuse a call of other heads than the handle's, or of a cache that was
+    closed after the call was made."""
+    if call.cache is not None and call.cache.c is None:
+        raise QgemvError(EINVAL, what, "the call's cache is closed")
     raise QgemvError(EINVAL, what, f"the call has heads {call.heads[0]} x {call.heads[1]}, "
                                    f"the handle is for {handle}")
 
@@ -687,7 +692,7 @@ def make_rope_call(q, k, positions, q_out=None, k_out=None, q_weight=None, k_wei
         a.cache = cache.c
         a.slots = _ints(slots, "slots", N, torch.int64)
         a.v, a.v_stride = _heads(v, "v", cache.kv_heads, D, N)
-    return _Call(a, (H, D), q, k, q_out, k_out, q_weight, k_weight, positions, cache, slots, v)
+    return _Call(a, (H, D), cache, q, k, q_out, k_out, q_weight, k_weight, positions, slots, v)
 
 
 class Rope:
@@ -709,8 +714,9 @@ class Rope:
             pass
 
     def run(self, call: _Call, stream=None):
-        if call.heads[1] != self.desc.head_dim:
-            _other_heads("qgemv_rope_run", call, f"heads of {self.desc.head_dim}")
+        if (call.heads[1] != self.desc.head_dim
+                or call.cache is not None and call.cache.c is None):
+            _unfit("qgemv_rope_run", call, f"heads of {self.desc.head_dim}")
         st = _lib.qgemv_rope_run(self.r, call.ref, _stream_ptr(stream))
         if st:
             _check(st, "qgemv_rope_run")
@@ -770,8 +776,8 @@ class Attn:
             pass
 
     def run(self, call: _Call, stream=None):
-        if call.heads != self.heads:
-            _other_heads("qgemv_attn_run", call, "%d x %d" % self.heads)
+        if call.heads != self.heads or call.cache.c is None:
+            _unfit("qgemv_attn_run", call, "%d x %d" % self.heads)
         st = _lib.qgemv_attn_run(self.a, call.ref, _stream_ptr(stream))
         if st:
             _check(st, "qgemv_attn_run")

@@ -36,9 +36,15 @@ def qg():
 
 @pytest.fixture
 def cache(qg):
-    c = object.__new__(qg.KVCache)
-    c.c, c.kv_heads, c.head_dim = None, 2, 64
-    return c
+    class Cache(qg.KVCache):
+        def __init__(self):
+            self.kv_heads, self.head_dim = 2, 64
+            self.c = 4096  # an address that nothing may look at
+
+        def close(self):
+            self.c = None
+
+    return Cache()
 
 
 def attn_call(qg, cache, N=1, H=4, D=64, **change):
@@ -94,3 +100,19 @@ def test_calls_of_other_heads_than_the_handle_are_refused(qg, cache):
     for slots in (None, ints(1, dtype=torch.int64)):
         with pytest.raises(ValueError):  # a cache, and no slots or no values
             qg.make_rope_call(half(1, 4, 64), half(1, 2, 64), ints(1), cache=cache, slots=slots)
+
+
+def test_calls_on_a_closed_cache_are_refused(qg, cache):
+    """A prepared call keeps the address of its cache's handle; once that is
+    closed, it does not go back to it."""
+    calls = [(qg.Attn, attn_call(qg, cache)),
+             (qg.Rope, qg.make_rope_call(half(1, 4, 64), half(1, 2, 64), ints(1), cache=cache,
+                                         slots=ints(1, dtype=torch.int64), v=half(1, 2, 64)))]
+    cache.close()
+    for cls, call in calls:
+        h = object.__new__(cls)
+        h.a = h.r = None
+        h.heads, h.desc = (4, 64), qg.rope_desc(64)
+        with pytest.raises(qg.QgemvError) as e:
+            h.run(call, stream=SimpleNamespace(cuda_stream=0))
+        assert e.value.status == -1 and "closed" in str(e.value)
