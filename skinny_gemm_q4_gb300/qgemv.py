@@ -425,9 +425,13 @@ def _stream_ptr(stream=None) -> int:
         return stream.cuda_stream
     if _raw_stream is None:
         import torch
-        raw, dev = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         torch.cuda.init()
-        _raw_stream = lambda: raw(dev())  # noqa: E731
+        raw, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream",
+                                                         "_cuda_getDevice"))
+        if raw and dev:
+            _raw_stream = lambda: raw(dev())  # noqa: E731
+        else:  # (they are not part of torch's public interface)
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
     return _raw_stream()
 
 

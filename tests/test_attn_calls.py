@@ -116,3 +116,12 @@ def test_calls_on_a_closed_cache_are_refused(qg, cache):
         with pytest.raises(qg.QgemvError) as e:
             h.run(call, stream=SimpleNamespace(cuda_stream=0))
         assert e.value.status == -1 and "closed" in str(e.value)
+
+
+def test_stream_without_torchs_private_queries(qg, monkeypatch):
+    """Where torch has no raw-stream query, its public one gives the stream."""
+    monkeypatch.setattr(qg, "_raw_stream", None)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "init", lambda: None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: SimpleNamespace(cuda_stream=77))
+    assert qg._stream_ptr() == 77 and qg._stream_ptr(SimpleNamespace(cuda_stream=5)) == 5
