@@ -373,6 +373,8 @@ void qgemv_chain_destroy(qg_chain *c);
  *   qgemv_attn_run     attention of every request's new tokens over its pages
  *
  * The pages end at the products; these entry points have no counterpart there.
+ * A handle belongs to the device that is current when it is made; a call while
+ * another is current, or with a cache of another device, is QG_EINVAL.
  *
  * Cache layout.  A pool of `pages` pages in device memory; a page holds
  * page_size tokens (16, 32, 64, 128 or 256) of every key/value head.  Token

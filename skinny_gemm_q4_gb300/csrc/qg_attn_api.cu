@@ -113,6 +113,24 @@ int few_tokens(const qg_attn_desc &d, int max_q)
     return std::max(1, std::min(max_q, kDecRows / (d.q_heads / d.kv_heads)));
 }
 
+// A handle's memory is on the device that it was made on: its launches go there only, and two
+// handles of a call are of one device.
+qg_status check_current(int device)
+{
+    int now = 0;
+    const cudaError_t e = cudaGetDevice(&now);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    if (now != device)
+        return fail(QG_EINVAL, "the handle was made on device %d, and device %d is current", device, now);
+    return QG_OK;
+}
+
+qg_status check_cache_device(const qg_kv *c, int device)
+{
+    if (c->device == device) return QG_OK;
+    return fail(QG_EINVAL, "the cache was made on device %d, the handle on device %d", c->device, device);
+}
+
 // One [N][heads][dim] fp16 argument: pointer (none for no tokens), alignment, token stride (0
 // becomes contiguous).
 qg_status check_heads(const char *name, const void *p, int64_t *stride, int heads, int dim,
@@ -252,6 +270,8 @@ qg_status qgemv_kv_write(qg_kv *c, const void *k, int64_t k_stride, const void *
     if (st != QG_OK) return st;
     if (!aligned(slots, 8)) return fail(QG_EALIGN, "slots is not 8-byte aligned");
     if (N == 0) return QG_OK;
+    st = check_current(c->device);
+    if (st != QG_OK) return st;
     RopeParams p = {};
     p.k = (const __half *)k;
     p.v = (const __half *)v;
@@ -274,6 +294,8 @@ qg_status qgemv_kv_read(qg_kv *c, const int64_t *slots, int64_t N, void *k_out, 
     if (st != QG_OK) return st;
     if (!aligned(slots, 8)) return fail(QG_EALIGN, "slots is not 8-byte aligned");
     if (N == 0) return QG_OK;
+    st = check_current(c->device);
+    if (st != QG_OK) return st;
     KvReadParams p = {};
     p.kv = view_of(c);
     p.slots = slots;
@@ -366,6 +388,8 @@ qg_status qgemv_rope_run(qg_rope *r, const qg_rope_args *a, void *stream)
         const qg_kv *c = a->cache;
         if (c->dim != D || c->heads != a->kv_heads)
             return fail(QG_EINVAL, "the cache has %d heads of %d", c->heads, c->dim);
+        st = check_cache_device(c, r->device);
+        if (st != QG_OK) return st;
         if (!a->slots && a->N > 0) return fail(QG_EINVAL, "null slots");
         if (!aligned(a->slots, 8)) return fail(QG_EALIGN, "slots is not 8-byte aligned");
         st = check_heads("v", a->v, &p.vs, a->kv_heads, D, a->N);
@@ -377,6 +401,8 @@ qg_status qgemv_rope_run(qg_rope *r, const qg_rope_args *a, void *stream)
         p.nv = a->kv_heads;
     }
     if (a->N == 0) return QG_OK;
+    st = check_current(r->device);
+    if (st != QG_OK) return st;
     p.q = (const __half *)a->q;
     p.k = (const __half *)a->k;
     p.qo = (__half *)a->q_out;
@@ -464,6 +490,8 @@ qg_status qgemv_attn_run(qg_attn *h, const qg_attn_args *a, void *stream)
     if (!c) return fail(QG_EINVAL, "null cache");
     if (c->dim != d.head_dim || c->heads != d.kv_heads)
         return fail(QG_EINVAL, "the cache has %d heads of %d", c->heads, c->dim);
+    qg_status st = check_cache_device(c, h->device);
+    if (st != QG_OK) return st;
     if (a->N < 0 || a->N > d.max_tokens || a->B < 1 || a->B > d.max_batch)
         return fail(QG_EINVAL, "N = %lld of at most %d tokens, B = %d of at most %d requests",
                     (long long)a->N, d.max_tokens, a->B, d.max_batch);
@@ -473,7 +501,7 @@ qg_status qgemv_attn_run(qg_attn *h, const qg_attn_args *a, void *stream)
     if (a->window < 0) return fail(QG_EINVAL, "window = %d", a->window);
     if (!std::isfinite(a->scale)) return fail(QG_EINVAL, "scale is not finite");
     int64_t qs = a->q_stride, os = a->out_stride;
-    qg_status st = check_heads("q", a->q, &qs, d.q_heads, d.head_dim, a->N);
+    st = check_heads("q", a->q, &qs, d.q_heads, d.head_dim, a->N);
     if (st == QG_OK) st = check_heads("out", a->out, &os, d.q_heads, d.head_dim, a->N);
     if (st != QG_OK) return st;
     if (!a->q_start || !a->kv_len || !a->page_table)
@@ -485,6 +513,8 @@ qg_status qgemv_attn_run(qg_attn *h, const qg_attn_args *a, void *stream)
         return fail(QG_EINVAL, "page table: width %d, stride %lld", a->table_width,
                     (long long)a->table_stride);
     if (a->N == 0) return QG_OK;
+    st = check_current(h->device);
+    if (st != QG_OK) return st;
     AttnParams p = {};
     p.kv = view_of(c);
     p.q = (const __half *)a->q;

@@ -610,8 +610,9 @@ class KVCache:
         self.kind, self.page_size, self.kv_heads, self.head_dim = (kind, page_size, kv_heads,
                                                                    head_dim)
         self.pool = pool
-        self.c = qgemv_kv_create(kind, pool.shape[0], page_size, kv_heads, head_dim,
-                                 pool.data_ptr())
+        with torch.cuda.device(pool.device):  # the handle's own memory goes there too
+            self.c = qgemv_kv_create(kind, pool.shape[0], page_size, kv_heads, head_dim,
+                                     pool.data_ptr())
 
     @classmethod
     def new(cls, kind: int, pages: int, page_size: int, kv_heads: int, head_dim: int,
