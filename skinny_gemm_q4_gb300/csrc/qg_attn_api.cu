@@ -536,7 +536,9 @@ qg_status qgemv_attn_run(qg_attn *h, const qg_attn_args *a, void *stream)
     p.max_len = (int)std::min(d.max_len, (int64_t)a->table_width * c->page_size);
     p.scale = a->scale;
     p.causal = a->causal;
-    p.window = a->window;
+    // A window of max_len positions hides nothing: a call without one.  (What is left is at most
+    // 2^30 wide, so that the kernels' L - T - window fits 32 bits.)
+    p.window = a->window >= p.max_len ? 0 : a->window;
     p.err = h->err;
     p.ws_o = h->ws_o;
     p.ws_ml = h->ws_ml;
