@@ -395,6 +395,8 @@ void qgemv_chain_destroy(qg_chain *c);
  *     its sign such that the block's number of largest magnitude (the first of
  *     equal ones) gets a code <= 0;
  *     q = rint(x / (step * mult)) clipped to the code range.
+ * A row (one token of one head) with a NaN or an infinity is held as a step of
+ * NaN: it reads back as NaN throughout, and is NaN to what attends to it.
  * The 16-byte units of a row are stored in an order that depends on the
  * token's place t in its record (shared-memory banks and the tensor cores'
  * 128-byte swizzle): unit u of an fp16 row lies at (u / 8) * 2048 + t * 128 +
@@ -584,7 +586,8 @@ typedef struct qg_attn_args {
  * sees none (L = 0, positions below 0) gets zeros and lse = -inf.  What the
  * cache holds at or past L, or before every window of the request, never
  * reaches a result, NaN and infinities included; among the positions that some
- * of a request's new tokens see, K and V must be finite.
+ * of a request's new tokens see, K and V must be finite: one that is not makes
+ * the rows that see it NaN or infinite, and possibly others of the request.
  * Rows of requests with T * (q_heads / kv_heads) <= 32 (decode and verify) have
  * the same bits whatever else is in the call and however many of a request's
  * tokens it verifies at once (the split of a context goes by absolute

@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(32 * Chunk<KIND, D>::WARPS, 1)
                     if (j >= vlo && j < r.L) ck = lds_f(st) * ksc, vs = lds_f(st + 64);
                     float *sc = scales + (it & 3) * 384;
                     sc[tid] = ck;
-                    sc[128 + tid] = fmaxf(log2f(vs), -40.0f);
+                    sc[128 + tid] = fmaxf(log2f(vs), -40.0f) + (vs - vs);  // (a NaN stays one)
                     sc[256 + tid] = 1.0f / fmaxf(vs, 0x1p-40f);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(b_sc + 8 * (it & 3));

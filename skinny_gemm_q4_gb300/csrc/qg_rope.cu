@@ -46,9 +46,18 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8])
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Maxima that keep a NaN (fmaxf drops it).
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
 // Quantise and store one head's row (numbers 8 l .. 8 l + 7 in lane l of its D /
 // 8 lanes) as row `t` of a record; `live` is false for lanes whose row is not
-// stored (they take part in the shuffles).
+// stored (they take part in the shuffles).  A row with a NaN or an infinity gets a step of NaN and
+// multipliers of 0: every number of it stands for NaN.
 template <int KIND, int D>
 __device__ __forceinline__ void store_row(const float (&x)[8], int l, uint8_t *rec, int t, int which,
                                           bool live)
@@ -64,16 +73,16 @@ __device__ __forceinline__ void store_row(const float (&x)[8], int l, uint8_t *r
     bool flip = false;  // Q4: the block's first number of largest magnitude is positive
     if constexpr (KIND == KV_Q8) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[i]));
-        big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
+        for (int i = 0; i < 8; ++i) big = max_nan(big, fabsf(x[i]));
+        big = max_nan(big, __shfl_xor_sync(~0u, big, 1));
+        big = max_nan(big, __shfl_xor_sync(~0u, big, 2));
     } else {
         float up = 0.0f, down = 0.0f;  // largest positive, and negated negative, number
 #pragma unroll
-        for (int i = 0; i < 8; ++i) up = fmaxf(up, x[i]), down = fmaxf(down, -x[i]);
-        up = fmaxf(up, __shfl_xor_sync(~0u, up, 1)), down = fmaxf(down, __shfl_xor_sync(~0u, down, 1));
-        up = fmaxf(up, __shfl_xor_sync(~0u, up, 2)), down = fmaxf(down, __shfl_xor_sync(~0u, down, 2));
-        big = fmaxf(up, down);
+        for (int i = 0; i < 8; ++i) up = max_nan(up, x[i]), down = max_nan(down, -x[i]);
+        up = max_nan(up, __shfl_xor_sync(~0u, up, 1)), down = max_nan(down, __shfl_xor_sync(~0u, down, 1));
+        up = max_nan(up, __shfl_xor_sync(~0u, up, 2)), down = max_nan(down, __shfl_xor_sync(~0u, down, 2));
+        big = max_nan(up, down);
         flip = up > down;
         if (__any_sync(~0u, up == down)) {  // which comes first?
             bool has = false, pos = false;
@@ -88,8 +97,9 @@ __device__ __forceinline__ void store_row(const float (&x)[8], int l, uint8_t *r
     }
     float top = big;
 #pragma unroll
-    for (int o = 4; o < D / 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    const float d = __fdiv_rn(top, kTop * kMost);
+    for (int o = 4; o < D / 8; o <<= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, o));
+    float d = __fdiv_rn(top, kTop * kMost);
+    d += d - d;  // an infinity: NaN
     float m = d > 0.0f ? fminf(ceilf(__fdiv_rn(big, __fmul_rn(kTop, d))), kMost) : 0.0f;
     if (flip) m = -m;
     const float f = __fmul_rn(d, m);
@@ -98,7 +108,7 @@ __device__ __forceinline__ void store_row(const float (&x)[8], int l, uint8_t *r
     // divides.  (Added to 1.5 2^23, and 8 for Q4, a number rounds to the integer that its low bits
     // then hold.)
     constexpr float kInt = 12582912.0f + (KIND == KV_Q4 ? 8.0f : 0.0f);
-    const float inv = f != 0.0f ? __frcp_rn(f) : 0.0f;
+    const float inv = m != 0.0f ? __frcp_rn(f) : 0.0f;
     float r[8], off = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

@@ -21,3 +21,63 @@ def test_attn_widest_window(qg, kind, causal, Ts, Ls):
     for window in (2 ** 31 - 1, 2 ** 30, 400):
         got = b.run(causal, window)
         assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("kind", [ap.Q8, ap.Q4])
+@pytest.mark.parametrize("D,heads", [(128, 3), (64, 5)])
+def test_rows_that_are_not_finite_read_back_as_nan(qg, kind, D, heads):
+    """A NaN or an infinity makes its row (one token of one head) NaN; the rows
+    beside it keep their bits."""
+    t = torch()
+    rng = np.random.default_rng(22)
+    N, page = 24, 16
+    x = [rng.normal(size=(N, heads, D)).astype(np.float16) for _ in range(2)]
+    bad = [y.copy() for y in x]
+    hit = [np.zeros((N, heads), bool) for _ in range(2)]
+    for w in range(2):
+        for i, v in enumerate((np.nan, np.inf, -np.inf)):
+            for d in (0, 31, D - 1):
+                n, h = rng.integers(N), rng.integers(heads)
+                bad[w][n, h, d], hit[w][n, h] = v, True
+        bad[w][5, 1], hit[w][5, 1] = np.nan, True
+        bad[w][6, 0], hit[w][6, 0] = -np.inf, True
+        bad[w][7, 0, 3:5], hit[w][7, 0] = (np.inf, np.nan), True
+    slots = dev(rng.permutation(2 * page)[:N].astype(np.int64))
+    c = qg.KVCache.new(kind, 2, page, heads, D)
+    c.write(dev(x[0]), dev(x[1]), slots)
+    clean = [o.cpu().numpy() for o in c.read(slots)]
+    c.write(dev(bad[0]), dev(bad[1]), slots)
+    for got, want, h in zip(c.read(slots), clean, hit):
+        got = got.cpu().numpy()
+        assert np.all(np.isnan(got[h])) and np.array_equal(got[~h], want[~h])
+    # a NaN under the norm, written by the rotation's pass
+    r = qg.Rope(D)
+    k = rng.normal(size=(N, heads, D)).astype(np.float16)
+    k[3, 1, 7] = np.nan
+    ones = t.ones(D, device="cuda")
+    r.run(qg.make_rope_call(dev(k), dev(k), dev(np.arange(N, dtype=np.int32)), k_weight=ones,
+                            cache=c, slots=slots, v=dev(x[1])))
+    got = c.read(slots)[0].cpu().numpy()
+    hit = np.zeros((N, heads), bool)
+    hit[3, 1] = True
+    assert np.all(np.isnan(got[hit])) and np.all(np.isfinite(got[~hit]))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T", [1, 3, 40])
+@pytest.mark.parametrize("which", [0, 1])
+def test_attn_over_a_nan_is_nan(qg, kind, T, which):
+    """A key or value of NaN reaches every row that sees it, in whatever form it
+    is cached, and no row of a context that ends before it."""
+    b = Batch(qg, kind, 128, 16, 4, 1, [T], [200], seed=23)
+    at = 200 - T  # seen by all new tokens, the last before them
+    want = b.run()
+    rows = np.ones((1, 1, 128), np.float16)
+    kv = [rows.copy(), rows.copy()]
+    kv[which][:] = np.nan
+    b.cache.write(dev(kv[0]), dev(kv[1]), dev(b.slots[at:at + 1]))
+    out, _ = b.run()
+    assert np.all(np.isnan(out)) and np.all(np.isfinite(want[0]))
+    b.Ls = [at]
+    out, lse = b.run()
+    assert np.all(np.isfinite(out)) and np.all(np.isfinite(lse))
