@@ -309,8 +309,8 @@ __global__ void __launch_bounds__(32 * kDecWarps, Dec<KIND, D, NG>::CTAS)
     };
     const int g = lane >> 2, t = lane & 3;
     int slot = 0, phase = 0;
-    // (Q4: nibbles enter as n 2^-24)
-    const float sc2 = p.scale * 1.4426950408889634f * (KIND == KV_Q4 ? 16777216.0f : 1.0f);
+    // (Q4: K's codes enter as (n - 8) 2^-20)
+    const float sc2 = p.scale * 1.4426950408889634f * (KIND == KV_Q4 ? 1048576.0f : 1.0f);
     // token offset in a record of this lane's first score row (m index g; the other is 8 further)
     const int tok0 = QUANT ? frag_row(g) : g;
     // This lane's shared-memory offsets in a record.  fp16: ldmatrix rows of K and V (unit u of 64
@@ -371,8 +371,6 @@ __global__ void __launch_bounds__(32 * kDecWarps, Dec<KIND, D, NG>::CTAS)
                     } else {
                         const uint2 v = *reinterpret_cast<const uint2 *>(q + 16 * ks + 4 * t);
                         qf[gi][ks] = make_uint2(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632));
-                        // high nibbles stay in their place: 16 times as large
-                        if (ks & 1) qf[gi][ks] = make_uint2(hmul2(qf[gi][ks].x, 0x2C002C00u), hmul2(qf[gi][ks].y, 0x2C002C00u));
                     }
                 }
             }
@@ -511,9 +509,12 @@ __global__ void __launch_bounds__(32 * kDecWarps, Dec<KIND, D, NG>::CTAS)
                                 a[k + 4] = hsub2(__byte_perm(y, 0x64646464u, 0x4140), 0x64806480u);
                                 a[k + 6] = hsub2(__byte_perm(y, 0x64646464u, 0x4342), 0x64806480u);
                             } else {
-                                const uint32_t x = kw[kb][k][0], y = x >> 8;  // (n - 8) 2^-24, and 2^-20
-                                a[k] = hsub2(x & 0x000f000fu, 0x00080008u);
-                                a[k + 2] = hsub2(y & 0x000f000fu, 0x00080008u);
+                                // (n - 8) 2^-20: low nibbles are n 2^-24 and times 16, high ones lie as
+                                // 16 n 2^-24.  (Both as they lie, with q / 16 for the high ones, took
+                                // bits from a q below 2^-10.)
+                                const uint32_t x = kw[kb][k][0], y = x >> 8;
+                                a[k] = hfma2(x & 0x000f000fu, 0x4C004C00u, 0x80808080u);
+                                a[k + 2] = hfma2(y & 0x000f000fu, 0x4C004C00u, 0x80808080u);
                                 a[k + 4] = hsub2(x & 0x00f000f0u, 0x00800080u);
                                 a[k + 6] = hsub2(y & 0x00f000f0u, 0x00800080u);
                             }

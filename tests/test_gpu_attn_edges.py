@@ -81,3 +81,15 @@ def test_attn_over_a_nan_is_nan(qg, kind, T, which):
     b.Ls = [at]
     out, lse = b.run()
     assert np.all(np.isfinite(out)) and np.all(np.isfinite(lse))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Ts,Ls", [([1] * 20, [1] * 20), ([8, 8, 8], [8, 9, 200]),
+                                   ([40, 33], [40, 90])])
+def test_attn_small_queries(qg, kind, Ts, Ls):
+    """Queries at fp16's smallest normal numbers, with a scale that makes scores
+    of ordinary size of them: every bit of q counts.  (Over one key the log
+    of the sum is the score.)"""
+    b = Batch(qg, kind, 128, 16, 4, 1, Ts, Ls, seed=24)
+    b.q = (b.q.astype(np.float64) * 2.0 ** -13).astype(np.float16)
+    b.check(scale=2.0 ** 10)
