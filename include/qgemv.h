@@ -596,7 +596,7 @@ typedef struct qg_attn_args {
  * The lengths are read on the device (one captured graph serves all steps).
  * A page number past the pool reads page 0, a length past the table or max_len
  * is cut, a request longer than max_q loses its tail: each sets bit 8 of
- * qgemv_attn_status; bits 1 and 2: a wait ran out (results undefined).
+ * qgemv_attn_status; bit 1: a wait ran out (results undefined).
  * Enqueued on stream, no synchronization.  (The pages have no counterpart.)
  * Errors: QG_EINVAL (null, sizes beyond the handle's, a cache of another
  * shape), QG_EALIGN, QG_ECUDA. */

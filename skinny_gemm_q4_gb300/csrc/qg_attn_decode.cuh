@@ -397,7 +397,9 @@ __global__ void __launch_bounds__(32 * kDecWarps, Dec<KIND, D, NG>::CTAS)
         }
 
         if (rec < r1) {
-            if (!mbar_wait(bars + 8 * slot, phase, 1u << 19)) {
+            // (a copy that lands between two lanes' last polls: the lanes go on or give up together)
+            const bool late = !mbar_wait(bars + 8 * slot, phase, 1u << 19);
+            if (__any_sync(~0u, late)) {
                 dead = true;
                 break;
             }

@@ -1,0 +1,16 @@
+"""What the attention kernels' source has to keep that no run can show."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "skinny_gemm_q4_gb300", "csrc")
+
+
+def test_the_few_row_kernel_gives_up_as_a_warp():
+    """A wait that ran out in some lanes only must not let the others go on to
+    the warp's shuffles and products: what leaves the loop over the records is a
+    vote, and lane 0, which reports it, takes part."""
+    with open(os.path.join(CSRC, "qg_attn_decode.cuh")) as f:
+        src = re.sub(r"//.*", "", f.read())
+    leave = re.findall(r"if \(([^{}]*)\) \{\s*dead = true;\s*break;", src)
+    assert len(leave) == 1 and "_sync(~0u" in leave[0]
