@@ -228,7 +228,8 @@ int64_t qgemv_row_bytes(qg_type t, int64_t K);
  * the kernel returns with undefined results (reflex-llm "docs/kernels.md",
  * uint32-loads section: a fault must never crash generation;
  * "docs/performance.md", Path C #29: a faulting kernel leaves the context
- * sticky).  Synchronous (a device-to-host copy of 4 bytes).  *flags_out == 0
+ * sticky).  Synchronous (waits for every stream of the device, then a copy of
+ * 4 bytes).  *flags_out == 0
  * means no kernel reported a problem.  Errors: QG_ECUDA. */
 qg_status qgemv_device_status(qg_handle *h, uint32_t *flags_out, int clear);
 
@@ -356,7 +357,8 @@ qg_status qgemv_chain_run_host(qg_chain *c, const qg_call *calls, int32_t ncalls
  * and 2 as for qgemv_device_status, bit 4: a wait for the earlier calls'
  * outputs ran out (results undefined); the kernel never traps (reflex-llm
  * "docs/kernels.md", uint32-loads section: a fault must never crash
- * generation).  Synchronous.  Errors: QG_EINVAL (null c), QG_ECUDA. */
+ * generation).  Synchronous, as qgemv_device_status.  Errors: QG_EINVAL (null
+ * c), QG_ECUDA. */
 qg_status qgemv_chain_status(qg_chain *c, uint32_t *flags_out, int clear);
 
 /* Free the chain's state (NULL is a no-op); the pages have no counterpart
@@ -445,7 +447,7 @@ qg_status qgemv_kv_read(qg_kv *c, const int64_t *slots, int64_t N, void *k_out, 
                         void *v_out, int64_t v_stride, void *stream);
 
 /* Read (and with clear != 0, reset) the cache's device error word (bit 8: a
- * slot past the pool).  Synchronous.  (The pages have no counterpart.)
+ * slot past the pool).  Synchronous, as qgemv_device_status.  (The pages have no counterpart.)
  * Errors: QG_EINVAL, QG_ECUDA. */
 qg_status qgemv_kv_status(qg_kv *c, uint32_t *flags_out, int clear);
 
@@ -603,7 +605,8 @@ typedef struct qg_attn_args {
 qg_status qgemv_attn_run(qg_attn *a, const qg_attn_args *args, void *stream);
 
 /* Read (and with clear != 0, reset) the handle's device error word.
- * Synchronous.  (The pages have no counterpart.)  Errors: QG_EINVAL, QG_ECUDA. */
+ * Synchronous, as qgemv_device_status.  (The pages have no counterpart.)
+ * Errors: QG_EINVAL, QG_ECUDA. */
 qg_status qgemv_attn_status(qg_attn *a, uint32_t *flags_out, int clear);
 
 /* Free the handle (NULL is a no-op).  No call on it may be in flight.  (The

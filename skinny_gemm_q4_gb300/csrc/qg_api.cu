@@ -935,6 +935,19 @@ qg_status run_with_scratch(qg_type t, int64_t M, int64_t K, const void *w_dev,
 
 // Sets the calling thread's qgemv_last_error text (used by qg_noalloc.cu).
 void set_last_error(const char *msg) { g_err = msg; }
+
+// Reads (and resets) a device error word, in order with every stream of the device: a null-stream
+// copy alone does not wait for streams made with cudaStreamNonBlocking.
+cudaError_t read_error_word(unsigned int *word, uint32_t *w, bool clear)
+{
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = cudaMemcpy(w, word, sizeof *w, cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess && clear && *w) {
+        e = cudaMemset(word, 0, sizeof *word);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+    }
+    return e;
+}
 }  // namespace qg
 
 namespace {
@@ -1290,13 +1303,9 @@ qg_status qgemv_device_status(qg_handle *h, uint32_t *flags_out, int clear)
     // NULL: the allocation-free entry point's error word on the current device.
     unsigned int *word = h ? h->err : noalloc_error_word();
     if (!word) return QG_ECUDA;
-    unsigned int w = 0;
-    cudaError_t e = cudaMemcpy(&w, word, sizeof w, cudaMemcpyDeviceToHost);
-    if (e != cudaSuccess) return cuda_fail(e, "error word read");
-    if (clear && w) {
-        e = cudaMemset(word, 0, sizeof(unsigned int));
-        if (e != cudaSuccess) return cuda_fail(e, "error word reset");
-    }
+    uint32_t w = 0;
+    const cudaError_t e = qg::read_error_word(word, &w, clear);
+    if (e != cudaSuccess) return cuda_fail(e, "error word");
     if (flags_out) *flags_out = w;
     return QG_OK;
 }
@@ -1462,13 +1471,9 @@ qg_status qgemv_chain_run_host(qg_chain *c, const qg_call *calls, int32_t ncalls
 qg_status qgemv_chain_status(qg_chain *c, uint32_t *flags_out, int clear)
 {
     if (!c) return fail(QG_EINVAL, "null chain");
-    unsigned int w = 0;
-    cudaError_t e = cudaMemcpy(&w, c->words + 2, sizeof w, cudaMemcpyDeviceToHost);
-    if (e != cudaSuccess) return cuda_fail(e, "chain error word read");
-    if (clear && w) {
-        e = cudaMemset(c->words + 2, 0, sizeof(unsigned int));
-        if (e != cudaSuccess) return cuda_fail(e, "chain error word reset");
-    }
+    uint32_t w = 0;
+    const cudaError_t e = qg::read_error_word(c->words + 2, &w, clear);
+    if (e != cudaSuccess) return cuda_fail(e, "chain error word");
     if (flags_out) *flags_out = w;
     return QG_OK;
 }

@@ -16,6 +16,7 @@ using namespace qg;
 
 namespace qg {
 void set_last_error(const char *msg);  // qg_api.cu: the text qgemv_last_error returns
+cudaError_t read_error_word(unsigned int *word, uint32_t *w, bool clear);  // qg_api.cu
 }
 
 struct qg_kv {
@@ -84,6 +85,7 @@ qg_status new_word(unsigned int **w)
     *w = nullptr;
     cudaError_t e = cudaMalloc((void **)w, sizeof(unsigned int));
     if (e == cudaSuccess) e = cudaMemset(*w, 0, sizeof(unsigned int));
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // (streams that do not wait for the null one)
     if (e == cudaSuccess) return QG_OK;
     cudaGetLastError();
     if (*w) cudaFree(*w);
@@ -93,8 +95,7 @@ qg_status new_word(unsigned int **w)
 
 qg_status read_word(unsigned int *w, uint32_t *flags_out, int clear)
 {
-    cudaError_t e = cudaMemcpy(flags_out, w, sizeof(uint32_t), cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess && clear) e = cudaMemset(w, 0, sizeof(uint32_t));
+    const cudaError_t e = read_error_word(w, flags_out, clear != 0);
     return e == cudaSuccess ? QG_OK : cuda_fail(e, "error word");
 }
 
@@ -351,6 +352,7 @@ qg_status qgemv_rope_create(qg_rope **out, const qg_rope_desc *d)
         return fail(QG_ENOMEM, "frequency table: %s", cudaGetErrorName(e));
     }
     e = cudaMemcpy(r->freq, turns, sizeof turns, cudaMemcpyHostToDevice);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
     if (e != cudaSuccess) {
         cudaFree(r->freq);
         delete r;

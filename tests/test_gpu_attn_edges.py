@@ -93,3 +93,30 @@ def test_attn_small_queries(qg, kind, Ts, Ls):
     b = Batch(qg, kind, 128, 16, 4, 1, Ts, Ls, seed=24)
     b.q = (b.q.astype(np.float64) * 2.0 ** -13).astype(np.float16)
     b.check(scale=2.0 ** 10)
+
+
+def test_status_waits_for_every_stream(qg):
+    """The status calls see what was enqueued before them on a stream that
+    does not wait for the null stream."""
+    t = torch()
+    c = qg.KVCache.new(qg.KV_Q8, 2, 16, 1, 64)
+    k = t.ones((1, 1, 64), dtype=t.float16, device="cuda")
+    slots = dev(np.array([1 << 20], np.int64))
+    a = qg.Attn(1, 1, 64, 1, 32, 1)
+    o = t.empty_like(k)
+    call = qg.make_attn_call(c, k, o, dev(np.array([0, 1], np.int32)),
+                             dev(np.array([16], np.int32)), dev(np.array([[1 << 20]], np.int32)), 1)
+    big = t.ones((8192, 8192), dtype=t.float16, device="cuda")
+    side = t.cuda.Stream()
+    with t.cuda.stream(side):
+        big @ big
+    t.cuda.synchronize()
+    for run, status in ((lambda: c.write(k, k, slots, stream=side), c.status),
+                        (lambda: a.run(call, stream=side), a.status)):
+        run()  # (a kernel's first launch may wait by itself)
+        assert status(clear=True) == 8 and status() == 0
+        with t.cuda.stream(side):
+            for _ in range(20):  # some 10 ms
+                big @ big
+            run()
+        assert status(clear=True) == 8 and status() == 0
