@@ -553,10 +553,13 @@ typedef struct qg_attn qg_attn;
 
 /* A handle on attention of one shape; layers share it (calls on it must be
  * ordered on one stream: they share its workspace).  It owns an error word and
- * a workspace for the partial results of long contexts, of max_batch *
- * min(max_tokens, 32 kv_heads / q_heads) * q_heads * (max_len / 512 + 48)
- * * (4 head_dim + 8) bytes at most: give max_batch no larger than needed.  (The pages have
- * no counterpart.)  Errors: QG_EINVAL, QG_EUNSUPPORTED (head_dim, group),
+ * workspaces for the partial results of few rows over long contexts, of
+ *     min(max_tokens, max_batch * max(1, 32 kv_heads / q_heads))
+ *         * q_heads * (max_len / 512 + 48) * (4 head_dim + 8) bytes
+ * at most (none up to max_len = 64), and of chunks, of 256 * (4 head_dim + 8)
+ * bytes for each SM (none where max_tokens * q_heads / kv_heads <= 32 or
+ * max_len < 512): give max_batch and max_len no larger than needed.  (The pages
+ * have no counterpart.)  Errors: QG_EINVAL, QG_EUNSUPPORTED (head_dim, group),
  * QG_ENOMEM, QG_ECUDA. */
 qg_status qgemv_attn_create(qg_attn **a, const qg_attn_desc *d);
 

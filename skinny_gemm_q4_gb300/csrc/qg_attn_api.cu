@@ -40,7 +40,7 @@ struct qg_attn {
     unsigned int *err;
     float *ws_o;    // partial results of contexts cut into leaves (null: one leaf at most)
     float2 *ws_ml;
-    float *wj_o;    // partial results of keys cut into parts (null: chunks never come)
+    float *wj_o;    // partial results of keys cut into parts (null: they never are)
     float2 *wj_ml;
 };
 
@@ -460,7 +460,8 @@ qg_status qgemv_attn_create(qg_attn **out, const qg_attn_desc *d)
     }
     if (attn_leaves(d->max_len) > 1) {
         const int few_q = few_tokens(*d, d->max_tokens);
-        const size_t rows = (size_t)d->max_batch * few_q * d->q_heads * attn_leaves(d->max_len);
+        const size_t tokens = std::min((size_t)d->max_batch * few_q, (size_t)d->max_tokens);
+        const size_t rows = tokens * d->q_heads * attn_leaves(d->max_len);
         e = cudaMalloc((void **)&a->ws_o, rows * d->head_dim * sizeof(float));
         if (e == cudaSuccess) e = cudaMalloc((void **)&a->ws_ml, rows * sizeof(float2));
         if (e != cudaSuccess) {
@@ -469,8 +470,9 @@ qg_status qgemv_attn_create(qg_attn **out, const qg_attn_desc *d)
             return fail(QG_ENOMEM, "attention workspace of %zu rows failed", rows);
         }
     }
-    if ((int64_t)d->max_tokens * (d->q_heads / d->kv_heads) > kDecRows) {
-        // keys are cut only while the CTAs, of at most 256 rows each, do not fill the GPU
+    if ((int64_t)d->max_tokens * (d->q_heads / d->kv_heads) > kDecRows && d->max_len >= 512) {
+        // keys are cut (into parts of 256 at least) only while the CTAs, of at most 256 rows each,
+        // do not fill the GPU
         const size_t rows = (size_t)256 * a->sms;
         e = cudaMalloc((void **)&a->wj_o, rows * d->head_dim * sizeof(float));
         if (e == cudaSuccess) e = cudaMalloc((void **)&a->wj_ml, rows * sizeof(float2));
@@ -546,6 +548,7 @@ qg_status qgemv_attn_run(qg_attn *h, const qg_attn_args *a, void *stream)
     p.ws_ml = h->ws_ml;
     p.few_q = few_tokens(d, a->max_q);
     p.few_leaves = attn_leaves(p.max_len);
+    p.by_token = a->N < (int64_t)a->B * p.few_q;
     p.row_parts = (p.few_q * p.group + 15) / 16;
     // Requests of few rows and the others go to different kernels; the host knows the sizes
     // when there is one request, or when all are of max_q tokens.

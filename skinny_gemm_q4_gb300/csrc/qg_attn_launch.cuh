@@ -40,10 +40,11 @@ struct AttnParams {
     float scale;
     int causal, window;
     unsigned int *err;
-    // partial results of contexts cut into leaves: [request][token < few_q][head][leaf]
+    // partial results of contexts cut into leaves: [token's row][head][leaf], the row being the
+    // token's among all of the call (by_token) or request * few_q + its place, whichever are fewer
     float *ws_o;                  // sum of p v, D numbers
     float2 *ws_ml;                // (m, sum of p), m in units of log2
-    int few_q, few_leaves;
+    int few_q, few_leaves, by_token;
     int few_max;                  // most rows of a request that the decode kernel takes in this call
     int row_parts;                // of 16 rows each
     // partial results of keys cut into parts: [token][head][part]

@@ -760,7 +760,8 @@ def make_attn_call(cache: KVCache, q, out, q_start, kv_len, page_table, max_q: i
 
 class Attn:
     """Attention of one head shape; layers share it on one stream.  Its workspace
-    grows with max_batch (default: max_tokens) times max_len."""
+    grows with max_len times the new tokens that requests of few rows can have
+    in a call: max_batch (default: max_tokens) requests, max_tokens at most."""
 
     def __init__(self, q_heads: int, kv_heads: int, head_dim: int, max_tokens: int,
                  max_len: int, max_batch: int = None):

@@ -120,3 +120,50 @@ def test_status_waits_for_every_stream(qg):
                 big @ big
             run()
         assert status(clear=True) == 8 and status() == 0
+
+
+@pytest.mark.parametrize("args", [(8, 2, 64, 2048, 65536), (32, 8, 128, 128, 128),
+                                  (4, 4, 128, 64, 4096, 64), (32, 8, 128, 4096, 8192, 1)])
+def test_attn_workspace_is_what_a_call_can_need(qg, args):
+    """No more device memory than the header states."""
+    t = torch()
+    H, Hkv, D, tokens, length, batch = (*args, args[3])[:6]
+    few = max(1, min(tokens, 32 * Hkv // H))
+    rows = min(tokens, batch * few) * H * (length // 512 + 48)
+    parts = 256 * t.cuda.get_device_properties(0).multi_processor_count
+    stated = rows * (4 * D + 8) * (length > 64)
+    stated += parts * (4 * D + 8) * (tokens * H // Hkv > 32 and length >= 512)
+    qg.Attn(1, 1, 64, 1, 16, 1)  # the library's own start-up
+    t.cuda.synchronize()
+    before = t.cuda.mem_get_info()[0]
+    a = qg.Attn(*args)
+    used = before - t.cuda.mem_get_info()[0]
+    assert used <= stated + 5 * (2 << 20)  # five allocations, in pages of 2 MiB
+    a.close()
+
+
+@pytest.mark.parametrize("kind", [ap.F16, ap.Q4])
+def test_attn_partial_results_of_ragged_and_full_calls(qg, kind):
+    """Few rows of several pieces, with as many tokens as requests times the
+    most of one (8 each) and with fewer: the same bits for the same rows."""
+    b = Batch(qg, kind, 64, 16, 4, 1, [8, 8, 8], [700, 1300, 90], seed=28)
+    out, lse = b.check()
+    b.Ts = [8, 1, 3]
+    keep = np.r_[0:8, 15:16, 21:24]  # the last tokens of each request
+    b.q, b.start = b.q[keep], np.array([0, 8, 9, 12], np.int32)
+    got, gl = b.run()
+    assert np.array_equal(got, out[keep]) and np.array_equal(gl, lse[keep])
+
+
+def test_attn_few_rows_beside_many_tokens(qg):
+    """A batch of single tokens as large as the handle's tokens, and a handle
+    whose default batch is its tokens."""
+    t = torch()
+    B = 96
+    b = Batch(qg, ap.Q8, 64, 16, 4, 2, [1] * B, [1 + (37 * i) % 500 for i in range(B)], seed=29)
+    want = b.run()
+    a = qg.Attn(4, 2, 64, B, 4096)
+    o = t.empty((B, 4, 64), dtype=t.float16, device="cuda")
+    a.run(qg.make_attn_call(b.cache, dev(b.q), o, dev(b.start), dev(np.array(b.Ls, np.int32)),
+                            dev(b.table), 1))
+    assert a.status() == 0 and np.array_equal(o.cpu().numpy(), want[0])
