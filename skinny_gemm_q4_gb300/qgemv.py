@@ -705,6 +705,7 @@ class Rope:
 
     def __init__(self, head_dim: int, **desc):
         self.desc = rope_desc(head_dim, **{n: v for n, v in desc.items() if v is not None})
+        self.head_dim = head_dim  # (a field of desc costs 0.1 us a look)
         self.r = qgemv_rope_create(self.desc)
 
     def close(self):
@@ -719,9 +720,8 @@ class Rope:
             pass
 
     def run(self, call: _Call, stream=None):
-        if (call.heads[1] != self.desc.head_dim
-                or call.cache is not None and call.cache.c is None):
-            _unfit("qgemv_rope_run", call, f"heads of {self.desc.head_dim}")
+        if call.heads[1] != self.head_dim or call.cache is not None and call.cache.c is None:
+            _unfit("qgemv_rope_run", call, f"heads of {self.head_dim}")
         st = _lib.qgemv_rope_run(self.r, call.ref, _stream_ptr(stream))
         if st:
             _check(st, "qgemv_rope_run")

@@ -92,7 +92,7 @@ def test_calls_of_other_heads_than_the_handle_are_refused(qg, cache):
         for N in (1, 2):
             assert refused(a, attn_call(qg, cache, N, 4, 64))
     r = object.__new__(qg.Rope)
-    r.r, r.desc = None, qg.rope_desc(128)
+    r.r, r.head_dim = None, 128
     for N in (1, 2):
         assert refused(r, qg.make_rope_call(half(N, 4, 64), half(N, 2, 64), ints(N)))
     with pytest.raises(ValueError):  # other heads than the cache's
@@ -112,7 +112,7 @@ def test_calls_on_a_closed_cache_are_refused(qg, cache):
     for cls, call in calls:
         h = object.__new__(cls)
         h.a = h.r = None
-        h.heads, h.desc = (4, 64), qg.rope_desc(64)
+        h.heads, h.head_dim = (4, 64), 64
         with pytest.raises(qg.QgemvError) as e:
             h.run(call, stream=SimpleNamespace(cuda_stream=0))
         assert e.value.status == -1 and "closed" in str(e.value)
