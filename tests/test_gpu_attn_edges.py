@@ -167,3 +167,52 @@ def test_attn_few_rows_beside_many_tokens(qg):
     a.run(qg.make_attn_call(b.cache, dev(b.q), o, dev(b.start), dev(np.array(b.Ls, np.int32)),
                             dev(b.table), 1))
     assert a.status() == 0 and np.array_equal(o.cpu().numpy(), want[0])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,L", [(1, 16384), (1, 16385), (2, 16896), (8, 33001)])
+def test_attn_few_rows_over_long_contexts(qg, kind, T, L):
+    """Contexts that reach the largest pieces (512 tokens from 16384 on), whole
+    and behind windows that begin inside one and at its edge."""
+    b = Batch(qg, kind, 64, 64, 4, 1, [T], [L], seed=25)
+    b.check()
+    if L > 16896:
+        for window in (L - 16384, 600, 16000):
+            b.check(window=window)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attn_chunks_of_many_requests(qg, kind):
+    """More requests of many rows than a warp has lanes, empty ones and single
+    tokens among them."""
+    Ts = [9 + (7 * i) % 40 if i % 6 else i % 2 for i in range(75)]
+    Ls = [T + (13 * i) % 90 for i, T in enumerate(Ts)]
+    Batch(qg, kind, 64, 16, 4, 1, Ts, Ls, seed=26).check()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Ts,Ls", [([40], [40]), ([130], [700]), ([33, 1, 64], [400, 90, 64]),
+                                   ([1, 1], [1, 130])])
+@pytest.mark.parametrize("window", [0, 50])
+def test_attn_handle_wider_than_the_contexts(qg, kind, Ts, Ls, window):
+    """A handle and a page table for far longer contexts than the call's: the
+    keys' parts, most of them empty, are joined all the same."""
+    t = torch()
+    b = Batch(qg, kind, 128, 16, 4, 1, Ts, Ls, seed=27)
+    N = sum(Ts)
+    wide = np.full((len(Ts), 2048), -1, np.int32)
+    wide[:, :b.table.shape[1]] = b.table
+    o, ls = t.empty((N, 4, 128), dtype=t.float16, device="cuda"), t.empty((N, 4), device="cuda")
+    a = qg.Attn(4, 1, 128, 256, 32768, len(Ts))
+    a.run(qg.make_attn_call(b.cache, dev(b.q), o, dev(b.start), dev(np.array(Ls, np.int32)),
+                            dev(wide), max(Ts), window=window, lse=ls))
+    assert a.status() == 0
+    o, ls = o.cpu().numpy(), ls.cpu().numpy()
+    few, lse = b.run(window=window)
+    for i, (T, L) in enumerate(zip(Ts, Ls)):
+        n = slice(b.start[i], b.start[i + 1])
+        ref, rl, mag = ap.attention(b.q[n], b.K[i], b.V[i], T, L, 128 ** -0.5, True, window)
+        vmax = np.abs(b.V[i]).max()
+        check(o[n], ref, half_ulp(ref) + 2.0 ** -10 * mag + L * 2.0 ** -24 * vmax, f"request {i}")
+        if 4 * T <= 32:  # few rows: the same bits whatever the handle's limits
+            assert np.array_equal(o[n], few[n]) and np.array_equal(ls[n], lse[n])
