@@ -548,7 +548,9 @@ qg_status qgemv_attn_run(qg_attn *h, const qg_attn_args *a, void *stream)
     p.ws_ml = h->ws_ml;
     p.few_q = few_tokens(d, a->max_q);
     p.few_leaves = attn_leaves(p.max_len);
-    p.by_token = a->N < (int64_t)a->B * p.few_q;
+    const bool by_token = a->N < (int64_t)a->B * p.few_q;
+    p.row_q = by_token;
+    p.row_b = by_token ? 0 : p.few_q;
     p.row_parts = (p.few_q * p.group + 15) / 16;
     // Requests of few rows and the others go to different kernels; the host knows the sizes
     // when there is one request, or when all are of max_q tokens.

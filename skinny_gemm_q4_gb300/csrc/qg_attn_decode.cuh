@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, Dec<KIND, D, NG>::CTAS)
                 if (row >= rows) continue;
                 const int tr = token_of(row), h = kh * p.group + row - tr * p.group;
                 const int64_t n0 = q0 + tr;
-                const int64_t at = ((p.by_token ? n0 : (int64_t)b * p.few_q + tr) * p.heads + h) * p.few_leaves + c;
+                const int64_t at = ((int64_t)(q0 * p.row_q + b * p.row_b + tr) * p.heads + h) * p.few_leaves + c;
                 const float mx = m[gi][e2];
                 if (g == 0) {
                     if (!only)

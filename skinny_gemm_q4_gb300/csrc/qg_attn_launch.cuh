@@ -40,11 +40,12 @@ struct AttnParams {
     float scale;
     int causal, window;
     unsigned int *err;
-    // partial results of contexts cut into leaves: [token's row][head][leaf], the row being the
-    // token's among all of the call (by_token) or request * few_q + its place, whichever are fewer
+    // partial results of contexts cut into leaves: [row][head][leaf], token t's row being
+    // q_start * row_q + request * row_b + t: its place among the call's tokens (1, 0) or among few_q
+    // of each request (0, few_q), whichever are fewer rows
     float *ws_o;                  // sum of p v, D numbers
     float2 *ws_ml;                // (m, sum of p), m in units of log2
-    int few_q, few_leaves, by_token;
+    int few_q, few_leaves, row_q, row_b;
     int few_max;                  // most rows of a request that the decode kernel takes in this call
     int row_parts;                // of 16 rows each
     // partial results of keys cut into parts: [token][head][part]

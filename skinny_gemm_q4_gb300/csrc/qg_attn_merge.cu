@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(kMergeThreads) qg_attn_merge_kernel(const __gr
     if (t >= r.T || !few_rows(p, r.T)) return;
     const int c0 = leaf_of(r.lo(p)), c1 = leaf_of(max(r.L, 1) - 1) + 1;
     if (c1 - c0 <= 1) return;  // finished by the decode kernel
-    const int64_t at = (p.by_token ? (int64_t)(r.q0 + t) * p.heads + h : row) * p.few_leaves;
+    const int64_t at = ((int64_t)(r.q0 * p.row_q + b * p.row_b + t) * p.heads + h) * p.few_leaves;
     const float2 *const mls = p.ws_ml + at;
     // eight leaves' loads at once, the first eight before the maximum is known
     constexpr int U = 8;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kMergeThreads) qg_attn_merge_rows_kernel(const
     if (t >= r.T || !few_rows(p, r.T)) return;
     const int c0 = leaf_of(r.lo(p)), c1 = leaf_of(max(r.L, 1) - 1) + 1;
     if (c1 - c0 <= 1) return;
-    const int64_t at = (p.by_token ? (int64_t)(r.q0 + t) * p.heads + h : row) * p.few_leaves;
+    const int64_t at = ((int64_t)(r.q0 * p.row_q + b * p.row_b + t) * p.heads + h) * p.few_leaves;
     const float2 *const mls = p.ws_ml + at;
     float mx = -INFINITY;
     for (int c = c0 + lane; c < c1; c += 32) mx = fmaxf(mx, mls[c].x);
