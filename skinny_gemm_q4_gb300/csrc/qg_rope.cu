@@ -230,7 +230,7 @@ template <int D, int KIND, bool HALF>
 __global__ void __launch_bounds__(512) qg_rope_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int LPR = D / 8, RPW = 32 / LPR;
-    __shared__ float4 angles[D / 4];  // (cos, sin) of two pairs each
+    __shared__ __align__(16) float2 cs[D / 2];
     const int64_t n = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int l = lane % LPR;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(512) qg_rope_kernel(const __grid_constant__ Ro
             const uint64_t ph = (uint64_t)pos * p.freq[i];
             float sn, cn;
             sincospif((float)(int32_t)(ph >> 32) * 0x1p-31f, &sn, &cn);
-            reinterpret_cast<float2 *>(angles)[i] = make_float2(cn * p.mscale, sn * p.mscale);
+            cs[i] = make_float2(cn * p.mscale, sn * p.mscale);
         }
         __syncthreads();
     }
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(512) qg_rope_kernel(const __grid_constant__ Ro
             }
             // HALF: number 8 l + i is in pair (8 l + i) mod (rot / 2); else pair 4 l + i / 2
             const bool turn = 8 * l < p.rot;
-            const float4 *c4 = angles + (HALF ? 4 * min(l, mate) : 2 * l);
+            const float4 *c4 = reinterpret_cast<const float4 *>(cs) + (HALF ? 4 * min(l, mate) : 2 * l);
             float2 v[8];
 #pragma unroll
             for (int i = 0; i < (HALF ? 4 : 2); ++i) {

@@ -17,11 +17,11 @@ def test_the_few_row_kernel_gives_up_as_a_warp():
 
 
 def test_the_rotations_angles_are_aligned_as_they_are_read():
-    """They are read 16 bytes at a time, so their array is one of 16-byte
-    elements: a float2 array is aligned to 8 only."""
+    """They are read 16 bytes at a time: a float2 array by itself is aligned to
+    8 only."""
     with open(os.path.join(CSRC, "qg_rope.cu")) as f:
         src = re.sub(r"//.*", "", f.read())
-    arrays = dict((n, t) for t, n in re.findall(r"__shared__ (\w+) (\w+)\[", src))
+    arrays = {n: how for how, n in re.findall(r"__shared__ ([^;]*?)(\w+)\[", src)}
     read = re.findall(r"reinterpret_cast<const float4 \*>\((\w+)\)", src)
-    assert "float4" in arrays.values()
-    assert all(arrays[n] == "float4" for n in read if n in arrays)
+    assert arrays
+    assert all("__align__(16)" in arrays[n] or "float4" in arrays[n] for n in read if n in arrays)
