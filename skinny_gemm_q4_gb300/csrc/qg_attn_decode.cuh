@@ -8,8 +8,9 @@
 // copy a record: 8 KB fp16, 4.25 KB Q8, 2.25 KB Q4 at D = 128), and holds the running
 // maximum, sum and output of the leaf's rows in registers.  Nothing waits for another
 // warp.  Measured, with the merge: 32 contexts of up to 8192 tokens in Q8 (215 MB) 58 us, 3.7 TB/s;
-// two of 131072 in Q4 (302 MB) 95 us, 3.2 TB/s: issue slots 60-63 % busy (about 590 and 465
-// instructions a record, most of them the codes' decoding), DRAM 44-55 %.  (With the eight warps of a CTA sharing a chunk and merging it through shared
+// two of 131072 in Q4 (302 MB) 96 us, 3.1 TB/s: issue slots 61-63 % busy, about 590 and 472
+// instructions a record (a third of them the codes' decoding, then products, sums and masks, the
+// walk, the copies and the leaves' ends), DRAM 43-56 %.  (With the eight warps of a CTA sharing a chunk and merging it through shared
 // memory, 32 contexts of up to 8192 in Q8 took 103 us: a third of the time was spent
 // at the chunks' ends.)
 //

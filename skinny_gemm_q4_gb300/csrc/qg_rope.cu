@@ -1,8 +1,10 @@
 // Norm + rotation of q and k, and the paged cache's writes and reads.
 //
-// All of it moves heads of D fp16 numbers with a few flops each: bound by HBM (8192 tokens of 40
-// heads, 168 MB, 33.9 us: 4.9 TB/s); quantised, by its instructions (8191 tokens of 2 x 8 heads into
-// Q4 22 us and back 14 us, issue slots 62-66 % busy); single tokens by a launch (2.7 us).
+// All of it moves heads of D fp16 numbers with a few flops each, so the floor is HBM's: 8192 tokens of
+// 40 heads, 168 MB, 33.8 us, 4.97 TB/s, where issue slots are 63 % and DRAM 46 % busy and a warp's
+// turn is a chain of loads, shuffles and products.  Quantised it is bound by its instructions: 8191
+// tokens of 2 x 8 heads written in 20.5 (Q8), 21.4 us (Q4) and read in 16.1, 13.8 (issue slots
+// 62-67 % busy); in fp16 14.6 and 12.4 (floor 10.0).  Single tokens: a launch (2.7 us).
 // A block takes one token: D / 8 lanes hold a head (8 numbers, one 16-byte
 // access each), so a head's sum of squares, its rotation partners and its
 // quantisation maxima are shuffles inside 16 (D = 128) or 8 lanes, and a head
@@ -387,8 +389,10 @@ __global__ void __launch_bounds__(512) qg_kv_read_kernel(const __grid_constant__
 namespace {
 
 // A block per token.  Warps: what gives the GPU about 32 an SM, between a turn each and `most` turns
-// each.  Rotation: up to 20, so that cos, sin and the weights serve many heads (8192 tokens of 20
-// turns: 5 each 39.9 us, 10 34.2, 20 33.3); reading: the loads that a lane has in flight.
+// each.  Rotation: up to 20, so that cos, sin and the weights serve many heads while a token of very
+// many still has warps enough.  8192 tokens, most 5 / 10 / 20 / 40, us: 32 + 8 heads of 128 (20
+// turns) 40.0 / 34.9 / 33.9 / 33.9, 64 + 8 73 / 58 / 55 / 55, 96 + 8 125 / 85 / 77 / 76, 16 + 2 21.3
+// / 20.0 / 19.9 / 19.9, 12 + 12 of 64 the same in all.  Reading: the loads that a lane has in flight.
 template <class P, class K>
 cudaError_t launch_tokens(K kernel, const P &p, int64_t n, int turns, int most, int sms, cudaStream_t stream)
 {
