@@ -12,7 +12,7 @@
 // so that S of the next key tile is ready when a softmax ends: the softmaxes (about 1650 cycles a
 // key tile, 1000 of them for the 16384 exponentials) run under the products of 4 x 512 cycles at
 // D = 128.  Measured 2640 cycles a key tile, 352-394 us for a prompt of 8192 tokens and 32 heads
-// (by the box and its power): 1.40-1.56 PFLOP/s, tensor pipe 67 % busy; the rest is the waits between the products and, for
+// (by the card and its power): 1.40-1.56 PFLOP/s, tensor pipe 67 % busy; the rest is the waits between the products and, for
 // a CTA, 7000 cycles before its first product and 4700 after its last.  At D = 64 the softmaxes
 // bound it (2440 with windows; an S for each tile, which fits there: 2 % less).
 // Tensor memory holds it because a softmax takes S into registers at once: one S for

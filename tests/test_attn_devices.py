@@ -76,7 +76,7 @@ def test_caches_are_made_on_their_pools_device(qg, monkeypatch):
 
 @pytest.mark.gpu
 def test_calls_while_another_device_is_current_are_refused(qg):
-    """(A box has one GPU, so the handle says that it is another's.)"""
+    """(With one GPU at hand, the handle is made to say that it is another's.)"""
     import torch
     c = qg.KVCache.new(qg.KV_F16, 2, 16, 2, 64)
     k = torch.zeros((1, 2, 64), dtype=torch.float16, device="cuda")
